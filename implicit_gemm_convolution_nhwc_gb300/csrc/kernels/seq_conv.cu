@@ -53,11 +53,13 @@ struct ConvParams {
   int64_t strip, strips, vecs;
 };
 
-// N consecutive parameters stored as TW, 16-byte aligned where N TW are
-// multiples of 16 bytes.
-template <int N, typename TW>
+// N consecutive parameters stored as TW. By 16-byte loads where kVec says that
+// w and bias are 16-byte aligned (the host checked) and N TW are multiples of
+// 16 bytes; else one by one: four fp32 taps of one channel are 16 bytes too, but
+// stand wherever their element's alignment allows.
+template <bool kVec, int N, typename TW>
 __device__ __forceinline__ void load_params(const TW* p, float (&v)[N]) {
-  constexpr int U = N * sizeof(TW) % 16 == 0 ? 16 / (int)sizeof(TW) : 1;
+  constexpr int U = kVec && N * sizeof(TW) % 16 == 0 ? 16 / (int)sizeof(TW) : 1;
 #pragma unroll
   for (int k = 0; k < N; k += U) {
     const Pack<TW, U> q = load_pack<U>(p + k);
@@ -69,13 +71,14 @@ __device__ __forceinline__ void load_params(const TW* p, float (&v)[N]) {
 template <typename T, int V, int W>
 __device__ __forceinline__ void load_taps(const seq_conv_args& a, int64_t c0, float2 (&w)[W][kPairs<V>],
                                           float2 (&bias)[kPairs<V>]) {
+  constexpr bool kVec = V > 1;
   float wv[V * W], bv[V] = {};
   if (a.w_dtype == CONV_F32) {
-    load_params<V * W>(static_cast<const float*>(a.w) + c0 * W, wv);
-    if (a.bias) load_params<V>(static_cast<const float*>(a.bias) + c0, bv);
+    load_params<kVec>(static_cast<const float*>(a.w) + c0 * W, wv);
+    if (a.bias) load_params<kVec>(static_cast<const float*>(a.bias) + c0, bv);
   } else {
-    load_params<V * W>(static_cast<const T*>(a.w) + c0 * W, wv);
-    if (a.bias) load_params<V>(static_cast<const T*>(a.bias) + c0, bv);
+    load_params<kVec>(static_cast<const T*>(a.w) + c0 * W, wv);
+    if (a.bias) load_params<kVec>(static_cast<const T*>(a.bias) + c0, bv);
   }
 #pragma unroll
   for (int i = 0; i < kPairs<V>; ++i) {
