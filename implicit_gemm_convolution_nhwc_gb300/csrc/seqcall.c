@@ -2,12 +2,13 @@
  * tensors of a library call, writes its argument struct and makes it. The
  * same in Python took longer than a single token's kernel.
  *
- *   call(entry, stream, head, item, kind, shape, dtype, item, kind, ...) -> int
+ *   call(entry, stream, device, head, item, kind, shape, dtype, item, ...) -> int
  *
  * entry: the address of a conv_status (const void* args, void* stream)
- * function; head: the first bytes of its struct; then four values for each
- * further field of it, in order. Returns the call's status (>= 0), or -1 - i
- * where item i is not the tensor that its kind, shape and dtype ask for (the
+ * function; device: the CUDA device that all tensors have to be on; head: the
+ * first bytes of the struct; then four values for each further field of it, in
+ * order. Returns the call's status (>= 0), or -1 - i where item i is not the
+ * tensor that its kind, shape and dtype ask for, or is on another device (the
  * library is not called then).
  */
 #define PY_SSIZE_T_CLEAN
@@ -16,18 +17,18 @@
 #include <string.h>
 
 enum {
-  DENSE = 0,        /* a contiguous CUDA tensor or None: its pointer */
+  DENSE = 0,        /* a contiguous tensor or None: its pointer */
   VIEW = 1,         /* [n, l, c], c contiguous, or None: pointer, strides of n and l */
   TOKEN = 2,        /* [n, c], c contiguous, or None: pointer, stride of n, 0 */
   GROUPS = 3,       /* [n, l, g, s], g and s dense, or None: as VIEW */
   TOKEN_GROUPS = 4, /* [n, g, s], g and s dense: as TOKEN */
-  WORKSPACE = 5,    /* a contiguous CUDA tensor of any shape and type, or None: pointer, bytes */
+  WORKSPACE = 5,    /* a contiguous tensor of any shape and type, or None: pointer, bytes */
   NUMBER = 6        /* an int */
 };
 
 enum { MAX_BYTES = 1024, MAX_DIMS = 8 };
 
-static PyObject *s_dtype, *s_shape, *s_is_cuda, *s_stride, *s_data_ptr, *s_nbytes;
+static PyObject *s_dtype, *s_shape, *s_get_device, *s_stride, *s_data_ptr, *s_nbytes;
 
 /* The ints of a tuple; their count, or -1. */
 static int read_ints(PyObject* t, int64_t* v) {
@@ -40,11 +41,13 @@ static int read_ints(PyObject* t, int64_t* v) {
   return n;
 }
 
-static int is_cuda(PyObject* t) {
-  PyObject* c = PyObject_GetAttr(t, s_is_cuda);
-  const int yes = c == Py_True;
-  Py_XDECREF(c);
-  return c ? yes : -1;
+/* The tensor's CUDA device (-1: it is not on one), or -2 with a Python error. */
+static long device_of(PyObject* t) {
+  PyObject* o = PyObject_CallMethodNoArgs(t, s_get_device);
+  if (!o) return -2;
+  const long v = PyLong_AsLong(o);
+  Py_DECREF(o);
+  return v == -1 && PyErr_Occurred() ? -2 : v;
 }
 
 /* The tensor's shape and strides; the number of dimensions, or -1. */
@@ -81,7 +84,7 @@ static int dense_from(int d, int n, const int64_t* size, const int64_t* stride) 
 
 /* One item into `to`: the bytes written; 0 where it is not what is asked for;
  * -1 with a Python error. */
-static int put(PyObject* t, long kind, PyObject* shape, PyObject* dtype, uint8_t* to) {
+static int put(PyObject* t, long device, long kind, PyObject* shape, PyObject* dtype, uint8_t* to) {
   int64_t out[3] = {0, 0, 0};
   const int bytes = kind == DENSE || kind == NUMBER ? 8 : kind == WORKSPACE ? 16 : 24;
   if (kind == NUMBER) {
@@ -89,9 +92,9 @@ static int put(PyObject* t, long kind, PyObject* shape, PyObject* dtype, uint8_t
     if (out[0] == -1 && PyErr_Occurred()) return -1;
   } else if (t != Py_None) {
     int64_t size[MAX_DIMS], stride[MAX_DIMS], want[MAX_DIMS];
-    const int cuda = is_cuda(t);
-    if (cuda < 0) return -1;
-    if (!cuda) return 0;
+    const long on = device_of(t);
+    if (on == -2) return -1;
+    if (on != device) return 0;
     const int n = layout(t, size, stride);
     if (n < 0) return PyErr_Occurred() ? -1 : 0;
     if (kind == WORKSPACE) {
@@ -123,8 +126,9 @@ static int put(PyObject* t, long kind, PyObject* shape, PyObject* dtype, uint8_t
 
 static PyObject* seq_call(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   (void)self;
-  if (n < 3 || (n - 3) % 4 != 0 || !PyBytes_Check(args[2])) {
-    PyErr_SetString(PyExc_TypeError, "call(entry, stream, head, item, kind, shape, dtype, ...)");
+  enum { FIRST = 4 }; /* of the items */
+  if (n < FIRST || (n - FIRST) % 4 != 0 || !PyBytes_Check(args[3])) {
+    PyErr_SetString(PyExc_TypeError, "call(entry, stream, device, head, item, kind, shape, dtype, ...)");
     return NULL;
   }
   union {
@@ -133,20 +137,21 @@ static PyObject* seq_call(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   } buf;
   void* entry = PyLong_AsVoidPtr(args[0]);
   void* stream = PyLong_AsVoidPtr(args[1]);
+  const long device = PyLong_AsLong(args[2]);
   if (PyErr_Occurred()) return NULL;
-  Py_ssize_t at = PyBytes_GET_SIZE(args[2]);
+  Py_ssize_t at = PyBytes_GET_SIZE(args[3]);
   if (at > MAX_BYTES) at = MAX_BYTES + 1;
-  else memcpy(buf.bytes, PyBytes_AS_STRING(args[2]), (size_t)at);
-  for (Py_ssize_t i = 3; i < n; i += 4) {
+  else memcpy(buf.bytes, PyBytes_AS_STRING(args[3]), (size_t)at);
+  for (Py_ssize_t i = FIRST; i < n; i += 4) {
     if (at + 24 > MAX_BYTES) {
       PyErr_SetString(PyExc_ValueError, "call: too many arguments");
       return NULL;
     }
     const long kind = PyLong_AsLong(args[i + 1]);
     if (kind == -1 && PyErr_Occurred()) return NULL;
-    const int wrote = put(args[i], kind, args[i + 2], args[i + 3], buf.bytes + at);
+    const int wrote = put(args[i], device, kind, args[i + 2], args[i + 3], buf.bytes + at);
     if (wrote < 0) return NULL;
-    if (wrote == 0) return PyLong_FromLong(-1 - (long)((i - 3) / 4));
+    if (wrote == 0) return PyLong_FromLong(-1 - (long)((i - FIRST) / 4));
     at += wrote;
   }
   int (*fn)(const void*, void*);
@@ -162,10 +167,10 @@ static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "seqcall", NULL, -1, 
 PyMODINIT_FUNC PyInit_seqcall(void) {
   s_dtype = PyUnicode_InternFromString("dtype");
   s_shape = PyUnicode_InternFromString("shape");
-  s_is_cuda = PyUnicode_InternFromString("is_cuda");
+  s_get_device = PyUnicode_InternFromString("get_device");
   s_stride = PyUnicode_InternFromString("stride");
   s_data_ptr = PyUnicode_InternFromString("data_ptr");
   s_nbytes = PyUnicode_InternFromString("nbytes");
-  if (!s_dtype || !s_shape || !s_is_cuda || !s_stride || !s_data_ptr || !s_nbytes) return NULL;
+  if (!s_dtype || !s_shape || !s_get_device || !s_stride || !s_data_ptr || !s_nbytes) return NULL;
   return PyModule_Create(&module);
 }

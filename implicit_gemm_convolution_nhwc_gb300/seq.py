@@ -2,7 +2,7 @@
 selective state-space scan and the root-mean-square norm, for prompts, training and single tokens.
 
 As in the package's other calls, the caller owns every tensor and the workspace, nothing is allocated or synchronised, and
-a failed check raises. Token tensors are [n, l, c] (single tokens: [n, c]) with the last dimension contiguous and any
+a failed check raises. All tensors of a call are on the current device (a library call launches there). Token tensors are [n, l, c] (single tokens: [n, c]) with the last dimension contiguous and any
 other strides, so a slice of a projection's output is used in place. The formulas, the meaning of `lengths` and of `slots`
 and the rules on overlap stand in the header.
 
@@ -42,6 +42,7 @@ _ZERO = (0, _NUMBER, None, None)
 
 _calls = {}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # torch.cuda.current_stream without its object
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _entry(name: str):
@@ -56,19 +57,28 @@ def _entry(name: str):
     return found
 
 
+def _device(x, name: str) -> int:
+    """x's device, which has to be the current one: the library launches, and asks for the number of SMs, there."""
+    device = x.get_device()
+    if device < 0:
+        raise ValueError(f"{name}: a CUDA tensor is required, got one on {x.device}")
+    if device != _current_device():
+        raise ValueError(f"{name}: on {x.device}, but the current device is cuda:{_current_device()}")
+    return device
+
+
 def _call(name: str, names, stream, x, head: bytes, *items):
     call, entry = _calls.get(name) or _entry(name)
-    if not x.is_cuda:
-        raise ValueError(f"{names[0]}: a CUDA tensor is required, got one on {x.device}")
-    handle = _raw_stream(x.get_device()) if stream is None and _raw_stream is not None else _stream(stream)
-    st = call(entry, handle, head, *items)
+    device = _device(x, names[0])
+    handle = _raw_stream(device) if stream is None and _raw_stream is not None else _stream(stream)
+    st = call(entry, handle, device, head, *items)
     if st > 0:
         raise ConvError(st, name)
     if st < 0:
         t, kind, shape, dtype = items[4 * (-1 - st):4 * (-st)]
         what = "" if kind == _WORKSPACE else f" {tuple(shape)} of {dtype},"
-        raise ValueError(f"{names[-1 - st]}: a CUDA tensor{what} {_LAYOUT[kind]}, is required, got {tuple(t.shape)} of "
-                         f"{t.dtype} on {t.device} with strides {t.stride()}")
+        raise ValueError(f"{names[-1 - st]}: a tensor{what} {_LAYOUT[kind]}, on cuda:{device} is required, got "
+                         f"{tuple(t.shape)} of {t.dtype} on {t.device} with strides {t.stride()}")
 
 
 def _bytes(name: str, *sizes) -> int:
@@ -190,6 +200,7 @@ def scan_workspace_bytes(n: int, l: int, c: int, s: int, g: int = 1, backward: b
 
 def scan_workspace(x, B, backward: bool = False):
     """The workspace for x [n, l, c] and B [n, l, g, s]: of the forward pass, or one that serves both (backward=True)."""
+    _device(x, "x")
     return _scratch(scan_workspace_bytes(*x.shape, B.shape[3], B.shape[2], backward), x.device)
 
 

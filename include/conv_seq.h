@@ -14,7 +14,8 @@
  *    stride_n >= (l-1) stride_l + c, or the same with n and l exchanged.
  *    Pointers are aligned to their element; 16-byte aligned pointers and
  *    strides select the vector kernels, others run element by element.
- *  - States, weights and parameters are dense.
+ *  - States, weights and parameters are dense. All memory and the stream belong
+ *    to the current device.
  *  - Types: `dtype` (CONV_F32, CONV_BF16 or CONV_F16) is the type of the token
  *    tensors. All arithmetic, states of the scan and sums are in fp32; each
  *    output is rounded once (to nearest even) into its type. Gradients of
