@@ -156,7 +156,13 @@ static PyObject* seq_call(PyObject* self, PyObject* const* args, Py_ssize_t n) {
   }
   int (*fn)(const void*, void*);
   memcpy(&fn, &entry, sizeof fn);
-  return PyLong_FromLong(fn(buf.bytes, stream));
+  /* The launch may wait for room in the stream's queue, and what runs before
+   * it for the interpreter (a host function of the caller's). */
+  int status;
+  Py_BEGIN_ALLOW_THREADS
+  status = fn(buf.bytes, stream);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(status);
 }
 
 static PyMethodDef methods[] = {

@@ -2,6 +2,9 @@
 functions of this process in the library's place."""
 import ctypes
 import inspect
+import struct
+import threading
+import time
 
 import pytest
 import torch
@@ -124,3 +127,28 @@ def test_a_scan_workspace_is_sized_for_the_tensors_device(monkeypatch):
     monkeypatch.setattr(seq, "_current_device", lambda: 0, raising=False)
     with pytest.raises(ValueError, match="current device is cuda:0"):
         seq.scan_workspace(_t(N, L, C, device=1), _t(N, L, 1, S, device=1))
+
+
+def test_other_threads_run_while_the_library_is_called():
+    """A launch may wait for room in the stream's queue, and a host function in front of it for the interpreter: the lock is
+    not held meanwhile. nanosleep(const timespec*, timespec*) has the shape of an entry."""
+    call, _ = seq._entry("seq_conv_fwd")
+    sleep = ctypes.cast(ctypes.CDLL(None).nanosleep, ctypes.c_void_p).value
+    ticks, done = [], threading.Event()
+
+    def tick():
+        while not done.is_set():
+            ticks.append(time.monotonic())
+            time.sleep(0.005)
+
+    other = threading.Thread(target=tick)
+    other.start()
+    try:
+        begin = time.monotonic()
+        assert call(sleep, 0, 0, struct.pack("qq", 0, 400_000_000)) == 0
+        end = time.monotonic()
+    finally:
+        done.set()
+        other.join()
+    assert end - begin >= 0.4
+    assert sum(begin + 0.1 < t < end - 0.1 for t in ticks) > 3
