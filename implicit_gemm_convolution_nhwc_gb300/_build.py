@@ -4,6 +4,11 @@ the small CPython module of the sequence operators' binding with the C compiler.
 Each .cu under csrc/ compiles to an object in parallel; the objects link
 into one shared library under _build/. A rebuild happens only when a source
 or header is newer than the library.
+
+The module is apart: it needs a C compiler and Python's headers, which the
+library and the convolutions' binding do not, and belongs to one interpreter,
+whose tag its name carries. It is built with the rest by build_seqcall(), or
+when the sequence operators are first called.
 """
 from __future__ import annotations
 
@@ -21,7 +26,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libconv_igemm.so")
 SEQCALL_SRC = os.path.join(CSRC, "seqcall.c")
-SEQCALL = os.path.join(BUILD, "seqcall.so")
+SEQCALL = os.path.join(BUILD, "seqcall" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -46,22 +51,26 @@ def _deps() -> list[str]:
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(SEQCALL):
+    if not os.path.exists(LIB):
         return False
     t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in _deps()) and os.path.getmtime(SEQCALL) >= os.path.getmtime(SEQCALL_SRC)
+    return all(os.path.getmtime(d) <= t for d in _deps())
 
 
-def _compile_seqcall() -> None:
+def build_seqcall(force: bool = False) -> str:
+    if not force and os.path.exists(SEQCALL) and os.path.getmtime(SEQCALL) >= os.path.getmtime(SEQCALL_SRC):
+        return SEQCALL
     cc = shutil.which("cc") or shutil.which("gcc")
     if cc is None:
-        raise RuntimeError("no C compiler found: the binding's module needs one")
+        raise RuntimeError("no C compiler found: the module of the sequence operators' binding needs one")
+    os.makedirs(BUILD, exist_ok=True)
     tmp = SEQCALL + f".tmp{os.getpid()}"
     res = subprocess.run([cc, "-O2", "-std=c11", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
                           SEQCALL_SRC, "-o", tmp], capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"{cc} failed on {SEQCALL_SRC}:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, SEQCALL)
+    return SEQCALL
 
 
 def _compile(src: str, verbose_ptxas: bool) -> str:
@@ -82,7 +91,6 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    _compile_seqcall()
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=jobs or min(len(srcs), os.cpu_count() or 4)) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
@@ -97,3 +105,4 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
 if __name__ == "__main__":
     import sys
     print(build(force="--force" in sys.argv, verbose_ptxas="-v" in sys.argv))
+    print(build_seqcall(force="--force" in sys.argv))

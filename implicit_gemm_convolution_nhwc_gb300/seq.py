@@ -49,7 +49,7 @@ def _entry(name: str):
     """(the module's call, the address of a library function)."""
     if "call" not in _calls:
         lib = load()
-        spec = importlib.util.spec_from_file_location("seqcall", _build.SEQCALL)
+        spec = importlib.util.spec_from_file_location("seqcall", _build.build_seqcall())
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         _calls["lib"], _calls["call"] = lib, module.call

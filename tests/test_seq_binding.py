@@ -2,14 +2,17 @@
 functions of this process in the library's place."""
 import ctypes
 import inspect
+import os
 import struct
+import sysconfig
 import threading
 import time
 
 import pytest
 import torch
 
-from implicit_gemm_convolution_nhwc_gb300 import seq
+import implicit_gemm_convolution_nhwc_gb300 as cig
+from implicit_gemm_convolution_nhwc_gb300 import _build, seq
 
 
 class Stand:
@@ -152,3 +155,29 @@ def test_other_threads_run_while_the_library_is_called():
         other.join()
     assert end - begin >= 0.4
     assert sum(begin + 0.1 < t < end - 0.1 for t in ticks) > 3
+
+
+@pytest.fixture
+def no_module(monkeypatch, tmp_path):
+    """A machine without a C compiler, on which the binding's module was never built."""
+    cig.load()
+    which = _build.shutil.which
+    monkeypatch.setattr(_build.shutil, "which", lambda name, *a, **kw: None if name in ("cc", "gcc") else which(name, *a, **kw))
+    monkeypatch.setattr(_build, "SEQCALL", str(tmp_path / "seqcall.so"))
+    monkeypatch.setattr(seq, "_calls", {})
+
+
+def test_the_library_needs_no_c_compiler(no_module):
+    assert _build.up_to_date()
+    assert _build.build() == _build.LIB
+    assert cig.load(build_if_missing=False) is not None
+    assert cig.output_dims(cig.Problem(n=1, h=8, w=8, c=4, k=4)) == (8, 8)
+
+
+def test_the_sequence_operators_name_what_their_module_lacks(no_module):
+    with pytest.raises(RuntimeError, match="C compiler"):
+        seq._entry("seq_conv_fwd")
+
+
+def test_the_module_belongs_to_this_interpreter():
+    assert os.path.basename(_build.SEQCALL) == "seqcall" + sysconfig.get_config_var("EXT_SUFFIX")
