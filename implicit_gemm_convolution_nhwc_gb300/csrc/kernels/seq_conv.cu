@@ -359,7 +359,9 @@ __global__ void __launch_bounds__(kBwdThreads, 2) conv_bwd_kernel(const __grid_c
             if (j_state >= 0 && j_state < W - 1)
               unpack(load_pack<V>(static_cast<const T*>(a.dstate_out) + (i * (W - 1) + j_state) * a.c + c0), out);
           }
-          gather(u, out);
+          // Where none of the dv is inside nothing is added: weights that are
+          // not finite would make NaN of the zeros.
+          if (inside > 0 && t < inside + W - 1) gather(u, out);
           if (t >= W - 1) {
             store_pack(dx + u * sd, pack<T, V>(out));
           } else if (s == 0 && a.dstate) {
