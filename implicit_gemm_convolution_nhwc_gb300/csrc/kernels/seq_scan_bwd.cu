@@ -334,9 +334,11 @@ __global__ void __launch_bounds__(kScanThreads, LN <= 4 ? 4 : 2) scan_bwd_kernel
 #pragma unroll
       for (int m = 0; m < P; ++m) dA[m] = __fadd2_rn(dA[m], dAs[m]);
       __syncthreads();
-      // The CTA's dB and dC of these 16 tokens.
+      // The CTA's dB and dC of these 16 tokens; 0 past the length, where states
+      // or gradients that are not finite have made NaN of their products with 0.
       float* slab = p.dbc + ((w.block * a.n + w.i) * a.l + ts) * 2 * s;
       const int tokens = w.t1 - ts < CK ? (int)(w.t1 - ts) : CK;
+      const int valid = used - sub;
       if (s == SP) {
         for (int u = threadIdx.x * 4; u < tokens * 2 * SP; u += kScanThreads * 4) {
           float4 v = *reinterpret_cast<const float4*>(sred + u);
@@ -345,6 +347,7 @@ __global__ void __launch_bounds__(kScanThreads, LN <= 4 ? 4 : 2) scan_bwd_kernel
             const float4 o = *reinterpret_cast<const float4*>(sred + r * CK * 2 * SP + u);
             v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
           }
+          if (u / (2 * SP) >= valid) v = make_float4(0.f, 0.f, 0.f, 0.f);
           *reinterpret_cast<float4*>(slab + u) = v;
         }
       } else {
@@ -354,7 +357,7 @@ __global__ void __launch_bounds__(kScanThreads, LN <= 4 ? 4 : 2) scan_bwd_kernel
             float v = sred[u];
 #pragma unroll
             for (int r = 1; r < 4; ++r) v += sred[r * CK * 2 * SP + u];
-            slab[i * s + k] = v;
+            slab[i * s + k] = i / 2 < valid ? v : 0.f;
           }
         }
       }

@@ -30,3 +30,29 @@ def test_conv_gradients(dtype, c, l, lengths):
                 assert torch.equal(dst[i], torch.zeros_like(dst[i]) if arriving is None else kept[i])
         plain = [k for k in range(c) if k not in (1, 2, 3)]
         assert bool(torch.isfinite(dx[..., plain]).all()) and bool(torch.isfinite(dw[plain]).all())
+
+
+@pytest.mark.parametrize("dtype, c, s", [(BF16, 64, 16), (F32, 5, 3), (BF16, 16, 64)])
+@pytest.mark.parametrize("l, lengths", [(21, [5, 0, 21]), (333, [130, 47, 0])])
+def test_scan_gradients(dtype, c, s, l, lengths):
+    n = len(lengths)
+    g = Gen(l + s)
+    x, dt, dy = (g.normal(n, l, c, dtype=dtype).cuda() for _ in range(3))
+    B, C = (g.normal(n, l, 1, s, dtype=dtype).cuda() for _ in range(2))
+    A = -g.uniform(0.3, 1.0, c, s).cuda()
+    state, arriving = g.normal(n, c, s, dtype=F32).cuda(), g.normal(n, c, s, dtype=F32).cuda()
+    state[:, 1, 0], arriving[:, 2, 1], arriving[:, 0, 2] = INF, -INF, NAN
+    lens = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    y, end = torch.empty_like(x), torch.empty_like(state)
+    kept = seq.scan_checkpoints(x, B)
+    ws = ws_nan(seq.scan_workspace_bytes(n, l, c, s, 1, True))
+    seq.scan_fwd(x, dt, A, B, C, y, softplus=True, state=state, state_out=end, checkpoints=kept, lengths=lens, ws=ws)
+    dx, ddt, dB, dC = (torch.full_like(v, 3) for v in (x, dt, B, C))
+    dA, dst = torch.empty_like(A), torch.empty_like(state)
+    seq.scan_bwd(x, dt, A, B, C, dy, kept, dx, ddt, dA, dB, dC, softplus=True, dstate_out=arriving, dstate=dst, lengths=lens,
+                 ws=ws)
+    for i, ln in enumerate(lengths):
+        for name, v in dict(y=y, dx=dx, ddt=ddt, dB=dB, dC=dC).items():
+            assert bool((v[i, ln:] == 0).all()), (name, i)
+        if ln == 0:
+            assert torch.equal(end[i], state[i]) and torch.equal(dst[i].nan_to_num(), arriving[i].nan_to_num())
