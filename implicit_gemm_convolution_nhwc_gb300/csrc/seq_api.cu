@@ -24,11 +24,14 @@ bool product_fits(int64_t a, int64_t b, int64_t c, int64_t limit) {
 
 uint64_t round256(uint64_t v) { return (v + 255) / 256 * 256; }
 
-// A view of [n][l][width] tokens.
-conv_status check_view(const seq_tensor& t, int64_t n, int64_t l, int64_t width, int64_t size, bool output) {
+// A view of [n][l][width] tokens. The stride along a single sequence or token is
+// not used.
+conv_status check_view(seq_tensor t, int64_t n, int64_t l, int64_t width, int64_t size, bool output) {
   if (n == 0 || l == 0) return CONV_OK;
   if (!t.data) return CONV_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(t.data) % size != 0) return CONV_ERR_ALIGNMENT;
+  if (n == 1) t.stride_n = 0;
+  if (l == 1) t.stride_l = 0;
   if (t.stride_n < 0 || t.stride_l < 0) return CONV_ERR_INVALID_ARG;
   if (t.stride_n > kMaxElems || t.stride_l > kMaxElems) return CONV_ERR_OVERFLOW;
   if (!product_fits(n - 1, t.stride_n, 1, kMaxElems) || !product_fits(l - 1, t.stride_l, 1, kMaxElems))

@@ -9,7 +9,8 @@
  *  - Tensors are channels-last: [n][l][c] with the channels contiguous. A
  *    seq_tensor gives its strides over sequences and tokens in elements, so a
  *    part of a wider buffer (one half of a projection's output) is taken and
- *    written in place. Input strides are >= 0 (0 repeats a row or a token);
+ *    written in place. Input strides are >= 0 (0 repeats a row or a token; the
+ *    stride along a single sequence or token is not used);
  *    an output's rows may not overlap: stride_l >= c and
  *    stride_n >= (l-1) stride_l + c, or the same with n and l exchanged.
  *    Pointers are aligned to their element; 16-byte aligned pointers and

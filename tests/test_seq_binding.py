@@ -12,6 +12,7 @@ import pytest
 import torch
 
 import implicit_gemm_convolution_nhwc_gb300 as cig
+import test_seq_host as host
 from implicit_gemm_convolution_nhwc_gb300 import _build, seq
 
 
@@ -181,3 +182,15 @@ def test_the_sequence_operators_name_what_their_module_lacks(no_module):
 
 def test_the_module_belongs_to_this_interpreter():
     assert os.path.basename(_build.SEQCALL) == "seqcall" + sysconfig.get_config_var("EXT_SUFFIX")
+
+
+@pytest.mark.parametrize("name", ["seq_conv_step", "seq_scan_step", "seq_conv_fwd"])
+def test_strides_of_a_single_token_or_sequence_are_not_looked_at(name):
+    """They have no meaning there, and the steps' are documented as not used. (What passes the checks fails at the launch
+    here, where there is no GPU.)"""
+    any_stride = host._Tensor(host.PTR, -1 if name == "seq_conv_fwd" else 16, 16 if name == "seq_conv_fwd" else -3)
+    sizes = dict(n=1, l=2, c=16) if name == "seq_conv_fwd" else dict(n=2, l=1, c=16)
+    make = host._conv if "conv" in name else host._scan
+    views = ("x", "y") if "conv" in name else ("x", "dt", "z", "b", "cc", "y")
+    args = make(**sizes, state_out=host.PTR, n_slots=2, **{k: any_stride for k in views})
+    assert host._status(name, args) == cig.STATUS.index("CONV_ERR_CUDA")
