@@ -51,7 +51,8 @@ __device__ __forceinline__ ScanPlace scan_place(const ScanParams& p, int64_t seg
 template <typename T, int TT, int CH, int E>
 __device__ __forceinline__ void stage_tokens(uint8_t* dst, const seq_tensor& v, const ScanPlace& w, int64_t tb,
                                              int64_t tend, bool vec) {
-  constexpr int PR = CH / E, kBytes = E * (int)sizeof(T);
+  constexpr int PR = CH / E;
+  static_assert(E * sizeof(T) == 16, "a pack is one asynchronous copy");
   const T* base = static_cast<const T*>(v.data) + w.i * v.stride_n + tb * v.stride_l + w.c0;
   const int rows = tend - tb < TT ? (int)(tend - tb) : TT;
 #pragma unroll
@@ -63,14 +64,7 @@ __device__ __forceinline__ void stage_tokens(uint8_t* dst, const seq_tensor& v, 
     if (vec) {
       const bool in = row < rows && col < w.channels;
       if (!in) from = static_cast<const T*>(v.data);
-      if constexpr (kBytes % 16 == 0) {
-#pragma unroll
-        for (int b = 0; b < kBytes; b += 16)
-          cp_async16(to + b, reinterpret_cast<const uint8_t*>(from) + (in ? b : 0), in ? 16u : 0u);
-      } else {  // 8 bytes
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(smem_u32(to)), "l"(from), "r"(in ? 8u : 0u)
-                     : "memory");
-      }
+      cp_async16(to, from, in ? 16u : 0u);
     } else {
       T* out = reinterpret_cast<T*>(to);
 #pragma unroll
@@ -200,14 +194,14 @@ __device__ __forceinline__ void store_row(float* row, int k0, int s, const float
   }
 }
 
-// Plan and strides checked by the host: whether packs of E channels are
-// aligned and never straddle the end of a group.
+// Plan and strides checked by the host: whether packs of E channels (16 bytes)
+// are aligned and never straddle the end of a group.
 template <typename T>
 inline bool scan_vec(const seq_scan_args& a, int e, bool backward) {
-  const int64_t size = sizeof(T), unit = e * size < 16 ? e * size : 16;
+  const int64_t size = sizeof(T);
   auto ok = [&](const seq_tensor& t) {
-    return !t.data || (reinterpret_cast<uintptr_t>(t.data) % unit == 0 && t.stride_n * size % unit == 0 &&
-                       t.stride_l * size % unit == 0);
+    return !t.data || (reinterpret_cast<uintptr_t>(t.data) % 16 == 0 && t.stride_n * size % 16 == 0 &&
+                       t.stride_l * size % 16 == 0);
   };
   const bool v = a.c / a.g % e == 0 && ok(a.x) && ok(a.dt) && ok(a.z);
   return backward ? v && ok(a.dy) && ok(a.dx) && ok(a.ddt) && ok(a.dz) : v && ok(a.y);

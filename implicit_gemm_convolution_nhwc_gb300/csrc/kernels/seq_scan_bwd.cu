@@ -110,8 +110,8 @@ template <typename T, int NS_, int LN_>
 struct BwdTile {
   static constexpr int NS = NS_, LN = LN_, SP = NS * LN, CL = 32 / LN, CH = kScanThreads / LN;
   static constexpr int TT = 32, CK = kScanCheckpoint;
-  static constexpr int E = CH < 16 / (int)sizeof(T) ? CH : 16 / (int)sizeof(T);  // elements of a staged pack
-  static constexpr int PAIRS = TT * CH / 2 / kScanThreads;                       // pairs of channels of a thread
+  static constexpr int E = 16 / (int)sizeof(T);             // elements of a staged pack
+  static constexpr int PAIRS = TT * CH / 2 / kScanThreads;  // pairs of channels of a thread
   static constexpr int DP = CH + 4, YP = CH + 8;  // pitches: LN tokens of CL channels on different banks
   static constexpr int kTok = TT * CH * (int)sizeof(T), kBc = TT * SP * (int)sizeof(T);
   static constexpr int kStage = 4 * kTok + 2 * kBc;
@@ -123,7 +123,7 @@ struct BwdTile {
   static constexpr int kQA = kY + TT * YP * 4;      // [TT][YP]: G p . A2
   static constexpr int kRed = kQA + TT * YP * 4;    // [4][CK][2 SP]: a warp's dB, dC
   static constexpr int kBytes = kRed + 4 * CK * 2 * SP * 4;
-  static_assert(PAIRS >= 1 && kScanThreads % (CH / 2) == 0, "a thread keeps its pair of channels");
+  static_assert(CH >= E && PAIRS >= 1 && kScanThreads % (CH / 2) == 0, "a thread keeps its pair of channels");
 };
 
 template <typename T, int NS, int LN>
@@ -452,7 +452,7 @@ template <typename T, int NS_, int LN_>
 struct CarryTile {
   static constexpr int NS = NS_, LN = LN_, SP = NS * LN, CH = kScanThreads / LN;
   static constexpr int TT = 16, G = LN < 8 ? 8 : LN;
-  static constexpr int E = CH < 16 / (int)sizeof(T) ? CH : 16 / (int)sizeof(T);
+  static constexpr int E = 16 / (int)sizeof(T);
   static constexpr int kTok = TT * CH * (int)sizeof(T), kBc = TT * SP * (int)sizeof(T);
   static constexpr int kStage = 3 * kTok + kBc, kC = 3 * kStage;  // [2][TT][SP] fp32
   static constexpr int kBytes = kC + 2 * TT * SP * 4;
