@@ -11,6 +11,10 @@
 // inside run without checks: with scalar arithmetic and a check a token the
 // forward took 103 us where it now takes 23 (8 x 2048 tokens of 2048 bf16
 // channels: 134 MB, 5.7 TB/s), the backward 163 us, now 40 (201 MB, 5.0 TB/s).
+// (The forward's 128 registers spill 12 bytes a thread with SiLU and four taps of
+// eight 16-bit channels; the backward's 127 do not spill.) Where 16 bytes do not
+// fit, by channels, strides or addresses, a thread has one channel and no loads
+// ahead, and issue bounds it: 49 and 115 us at 2046 channels.
 #include "seq_common.cuh"
 
 namespace cig {
@@ -421,7 +425,8 @@ bool vectors(const seq_conv_args& a, int v) {
 // 8 x 2048 tokens of 2048 channels left 16 % of the places empty: forward 25.4 us,
 // so 23.6 us; backward 55.7 us, so 49.8 us; 4 prompts of up to 4096 tokens by 4096
 // channels, 1.7 rounds, 55.3 us, so 51.1 us (all before loads went ahead; at most
-// 64 tokens: 46 us for those prompts against 43).
+// 64 tokens: 46 us for those prompts against 43). The places are those of 152 SMs
+// whatever the device, so that a workspace's size follows from the call's alone.
 constexpr int64_t kFwdPlaces = 152 * 4, kBwdPlaces = 152 * 2;
 template <class Ctas, class Strips>
 int64_t balanced_strip(int64_t l, int64_t least, int64_t places, Ctas ctas, Strips strips) {

@@ -24,8 +24,10 @@
 // instructions. No unit is full (issue 61 %, shared memory 59 %, fp32 39 %,
 // special functions 19 %); it is bound by the latencies along a token (the
 // recurrence, the exchanges), which four warps hide in part: at three CTAs an
-// SM it took a fifth longer. Letting the last segment, which needs nothing of the
-// first launch, start during it gained 2 us.
+// SM it took a fifth longer. The bound of 128 registers that four CTAs need
+// spills little: 48 bytes stored and 44 loaded a thread with four states a lane,
+// 28 and 44 with two. All segments wait for the first launch. The last one needs
+// nothing of it, but starting it early gained just 2 us and was not kept.
 //
 // The warps' sums meet in shared memory, the channel blocks' in one slab each
 // in the workspace. Everything is added in an order fixed by the sizes.

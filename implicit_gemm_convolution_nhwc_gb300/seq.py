@@ -216,7 +216,8 @@ def scan_checkpoints(x, B):
 def scan_fwd(x, dt, A, B, C, y, *, D=None, z=None, dt_bias=None, softplus=False, state=None, state_out=None,
              checkpoints=None, lengths=None, ws=None, stream=None):
     """h[t] = exp(delta A) h[t-1] + delta x B, y = (C . h + D x) silu(z) with delta = dt + dt_bias or its softplus, over
-    x, dt, z [n, l, c], B, C [n, l, g, s], A [c, s]. state and state_out are [n, c, s] in fp32."""
+    x, dt, z [n, l, c], B, C [n, l, g, s], A [c, s]. state and state_out are [n, c, s] in fp32 (16-byte aligned where s is a
+    multiple of 4, as all states of the scan)."""
     shape, bc, n, l, c, s, head = _scan_head(x, B, softplus, 3)
     dtype, kept, per = x.dtype, (n, c, s), (c,)
     _call("seq_scan_fwd", _SCAN_NAMES, stream, x, head, x, _VIEW, shape, dtype, dt, _VIEW, shape, dtype, z, _VIEW, shape, dtype,

@@ -14,7 +14,9 @@
  *    an output's rows may not overlap: stride_l >= c and
  *    stride_n >= (l-1) stride_l + c, or the same with n and l exchanged.
  *    Pointers are aligned to their element; 16-byte aligned pointers and
- *    strides select the vector kernels, others run element by element.
+ *    strides select the vector kernels, others run element by element. (The
+ *    scan's states and their gradients have to be 16-byte aligned where s is a
+ *    multiple of 4, its checkpoints and the workspaces always.)
  *  - States, weights and parameters are dense. All memory and the stream belong
  *    to the current device.
  *  - Types: `dtype` (CONV_F32, CONV_BF16 or CONV_F16) is the type of the token
